@@ -68,6 +68,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A row's running maximum moves only when a tile exceeds it by more than 2^8,
 // so weights stay below 2^8 and hardly a tile rescales anything.
 constexpr float kLazy = 8.0f;
+// Weights that carry no scale are stored times 2^kUp, a row's largest in 2^6 .. 2^14: an fp16
+// pair holds 22 bits of a weight from 2^-3 on, below that an absolute 2^-25, 2^-31 of the largest.  (Where
+// one token of small V takes most of the softmax, 8000 tokens, INT4 with 64-channel groups: 2.7e-3 of the
+// result with weights times 2^-6, 2.1e-4 with 2^6, which is the rounding of the output.)
+constexpr float kUp = 6.0f;
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 r;
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, RT>::kThreads, 1)
     const float qk_scale = a.sm_scale * s_fp8 * kLog2e;   // logits in log2 units
     // INT8 / INT4 weights carry V's scale (up to 65504 / 127 or / 7) and up to
     // 2^kLazy: the factor 2^kLogF keeps them inside fp16; sums carry it too
-    constexpr float kLogF = FMT == INT8 ? -2.f : (I4 ? -6.f : 0.f);
+    constexpr float kLogF = FMT == INT8 ? -2.f : (I4 ? -6.f : kUp);
     constexpr int SUB = (I4 && D == 64 && NG == 4) ? 2 : 1;   // scale groups inside a 16-byte chunk
     constexpr int CPG = NG == 1 ? CH : (CH >= NG ? CH / NG : 1);   // chunks per scale group
     // byte offset of this lane's row in chunk ch of a 32-row tile (rows = tokens)

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kCols = kUsed <= 256 ? 256 : 512;
     static_assert(kUsed <= 512, "tensor memory");
     constexpr uint32_t kIdS = idesc(128, RT, 0, 0), kIdO = idesc(128, 2 * RT, 1, 1), kIdLo = idesc(128, RT, 1, 1);
-    constexpr float kLogF = FMT == INT8 ? -2.f : (I4 ? -6.f : 0.f);      // see kvq_verify.cuh
+    constexpr float kLogF = kScaled && NG == 1 ? (I4 ? -6.f : -2.f) : kUp;   // see kvq_verify.cuh (group scales are in V)
     constexpr float kScaleUp = I4 ? 4.f : 64.f, kMaxScale = 65504.f / kScaleUp;   // V's group scales
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);

@@ -1,0 +1,72 @@
+"""kvq_verify_attention over the range of V: small rows, rows of very different size, and a token that takes most of
+the softmax.  The results are held to bounds that shrink with V (tests/verify_bound.py)."""
+import pytest
+import torch
+
+import fp8_int8_quantized_gb300 as kvq
+from tests import spec_ref as R
+from tests import verify_bound as VB
+from tests.test_gpu_verify import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    kvq.build()
+    torch.cuda.init()
+
+
+def fill(b, kind):
+    """Rewrites the batch's K, V and queries."""
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    if kind == "sink":   # the first tokens' logits lie 12 above the others', their V is 2^-8 as large
+        c = 12.0 * b.d ** 0.5 / 8.0
+        b.q[..., 0] = 8.0
+        b.k[..., 0] = 0.0
+        first = [sum(b.ctx[:i]) for i in range(len(b.ctx))]
+        b.k[first, :, 0] = c
+        b.v[first] *= 2.0 ** -8
+    elif kind == "mixed":   # every row its own size
+        e = torch.randint(0, 21, (b.v.shape[0], b.v.shape[1], 1), generator=gen, device="cuda")
+        b.v.copy_((b.v.float() * torch.exp2(-e.float())).half())
+    else:
+        b.v.copy_((b.v.float() * kind).half())
+    kvq.append(b.k, b.v, b.cache, b.slots, b.scale)
+
+
+def check(b, out, seqs):
+    for i in seqs:
+        k, v = b.kv(i)
+        at = sum(b.ctx[:i])
+        s = b.slots[at:at + b.ctx[i]]
+        if b.cache.v_scales is None:
+            unit, codes = torch.ones_like(v[..., 0]), v.abs()
+        else:
+            sc = b.cache.v_scales[s // b.bs, :, s % b.bs].double().reshape(*v.shape[:2], -1)
+            full = sc.repeat_interleave(b.d // sc.shape[-1], -1)
+            if sc.shape[-1] > 1 and b.d == 128:   # the scale is in V
+                unit, codes = torch.ones_like(v[..., 0]), v.abs()
+            else:
+                unit, codes = sc.amax(-1), torch.where(full > 0, v.abs() / full, 0.0)
+        q = b.q[b.start[i]:b.start[i + 1]].double()
+        pair = b.group and b.group < b.d and b.d == 128
+        o, bound = VB.attention(q, k, v, unit, codes, b.masks[i], b.d ** -0.5, b.ctx[i] - b.n[i], pair)
+        got = out[b.start[i]:b.start[i + 1]].double()
+        assert torch.isfinite(got).all()
+        far = ((got - o).abs() / bound).max().item()
+        assert far <= 1.0, (i, b.ctx[i], far)
+        e = VB.rms(got - o)
+        assert e <= VB.rms_bound(o), (i, b.ctx[i], e / VB.rms(o))
+    assert kvq.device_error_check() == (0, 0)
+
+
+@pytest.mark.parametrize("kind", [1.0, "sink"])
+@pytest.mark.parametrize("fmt,group,d", [("e4m3", 0, 128), ("e5m2", 0, 128), ("e4m3", 0, 64), ("e5m2", 0, 64), ("int8", 32, 128),
+                                         ("int8", 64, 128), ("int4", 32, 128), ("int4", 64, 128)])
+@pytest.mark.parametrize("hkv,g,n", [(2, 2, 3), (1, 8, 4), (1, 8, 7)])
+def test_one_token_takes_most_of_the_softmax(fmt, group, d, hkv, g, n, kind):
+    ctx = [8000, 700, 90, n]
+    b = Batch(ctx, [n] * 4, hkv, g, d, 16, fmt, group, tree=True, seed=31, outliers=False)
+    fill(b, kind)
+    check(b, b.run(), range(4))
