@@ -914,9 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     bar_any(1 + g, 128, false);
-                    if (tok < RT) {   // (a row that has seen nothing, or only NaN, keeps kNone)
+                    if (tok < RT) {
+                        // Only rows that exceed their own maximum by 2^kLazy: what the others hold does not
+                        // depend on tokens they do not see.  (One that has seen nothing, or only NaN, keeps kNone.)
                         const float old = mm[tok];
-                        const float mn = fmaxf(fmaxf(fmaxf(mx_s[tok], mx_s[RT + tok]), fmaxf(mx_s[2 * RT + tok], mx_s[3 * RT + tok])), old);
+                        const float tile = fmaxf(fmaxf(mx_s[tok], mx_s[RT + tok]), fmaxf(mx_s[2 * RT + tok], mx_s[3 * RT + tok]));
+                        const float mn = tile > old + kLazy ? tile : old;
                         f_s[g * RT + tok] = fast_exp2(old - mn);
                         m_s[g * RT + tok] = mn;
                     }

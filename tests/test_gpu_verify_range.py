@@ -70,3 +70,19 @@ def test_one_token_takes_most_of_the_softmax(fmt, group, d, hkv, g, n, kind):
     b = Batch(ctx, [n] * 4, hkv, g, d, 16, fmt, group, tree=True, seed=31, outliers=False)
     fill(b, kind)
     check(b, b.run(), range(4))
+
+
+@pytest.mark.parametrize("fmt,group,d", [("e4m3", 0, 128), ("int8", 0, 128), ("int4", 32, 128), ("e5m2", 0, 64), ("int8", 16, 64)])
+@pytest.mark.parametrize("g,n", [(2, 4), (8, 4), (8, 7)])
+def test_large_logits_of_a_draft_leave_its_siblings_alone(fmt, group, d, g, n):
+    """Draft 2's K grows by 40: its own query's logits do, and nothing of the others changes, to the bit."""
+    b = Batch([3000 + i for i in range(16)], [n] * 16, 8, g, d, 16, fmt, group, tree=True, seed=32, outliers=False)
+    masks = [1 | 1 << i for i in range(n)]   # all children of the first
+    mask = R.signed(masks * 16).cuda()
+    clean = b.run(tree_mask=mask)
+    at = torch.tensor([sum(b.ctx[:i + 1]) - n + 2 for i in range(16)], device="cuda")
+    b.k[at] = (b.k[at].float() * 40).half()
+    kvq.append(b.k, b.v, b.cache, b.slots, b.scale)
+    out = b.run(tree_mask=mask)
+    own = torch.arange(16 * n, device="cuda") % n == 2
+    assert torch.equal(out[~own], clean[~own]) and not torch.equal(out[own], clean[own])
