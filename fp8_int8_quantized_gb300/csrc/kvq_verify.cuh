@@ -68,11 +68,22 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A row's running maximum moves only when a tile exceeds it by more than 2^8,
 // so weights stay below 2^8 and hardly a tile rescales anything.
 constexpr float kLazy = 8.0f;
-// Weights that carry no scale are stored times 2^kUp, a row's largest in 2^6 .. 2^14: an fp16
-// pair holds 22 bits of a weight from 2^-3 on, below that an absolute 2^-25, 2^-31 of the largest.  (Where
-// one token of small V takes most of the softmax, 8000 tokens, INT4 with 64-channel groups: 2.7e-3 of the
-// result with weights times 2^-6, 2.1e-4 with 2^6, which is the rounding of the output.)
+// Weights are stored times 2^kUp, a row's largest in 2^6 .. 2^14: an fp16 pair holds 22 bits of a
+// weight from 2^-3 on, below that an absolute 2^-25, 2^-31 of the largest.  (Where one token of small V
+// takes most of the softmax, 8000 tokens, INT4 with 64-channel groups: 2.7e-3 of the result with
+// weights times 2^-6, 2.1e-4 with 2^6, which is the rounding of the output.)
 constexpr float kUp = 6.0f;
+// Where a weight carries its token's V scale, "largest" is that of the product: the running maximum is
+// of z + log2 |s_V| (the largest of the row's groups), so that the pair's range does not depend on how
+// large V is.  The sum of the weights without the scale is held in fp32 and takes the same factors.  (With
+// the maximum of z alone and fixed factors 2^-2 and 2^-6, INT8 and INT4, 8000 tokens: 2.4e-3 of
+// the result for V of 2^-7, 2e-2 for 2^-10; now 2.2e-4 and 9e-4, the rounding of the output.)
+// Bounded by 2^-40 (all values below fp16's smallest) and 2^40, NaN too: rows of zeros have scale 0.
+__device__ __forceinline__ float log2_scale(float s) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fabsf(s)));
+    return fminf(fmaxf(r, -40.f), 40.f);
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 r;
@@ -410,9 +421,6 @@ __global__ void __launch_bounds__(Shape<FMT, D, RT>::kThreads, 1)
 
     const float s_fp8 = (!kScaled && a.scale) ? __ldg(a.scale) : 1.0f;
     const float qk_scale = a.sm_scale * s_fp8 * kLog2e;   // logits in log2 units
-    // INT8 / INT4 weights carry V's scale (up to 65504 / 127 or / 7) and up to
-    // 2^kLazy: the factor 2^kLogF keeps them inside fp16; sums carry it too
-    constexpr float kLogF = FMT == INT8 ? -2.f : (I4 ? -6.f : kUp);
     constexpr int SUB = (I4 && D == 64 && NG == 4) ? 2 : 1;   // scale groups inside a 16-byte chunk
     constexpr int CPG = NG == 1 ? CH : (CH >= NG ? CH / NG : 1);   // chunks per scale group
     // byte offset of this lane's row in chunk ch of a 32-row tile (rows = tokens)
@@ -609,13 +617,27 @@ __global__ void __launch_bounds__(Shape<FMT, D, RT>::kThreads, 1)
                                 if (!((word[n] >> (8 * j + 2 * c + e)) & 1u)) s[n >> 1][j][2 * (n & 1) + e] = -INFINITY;
                     }
                 }
-                // ---- running maximum, weights, sums
+                // ---- running maximum (of the weights with V's scale), weights, sums
+                [[maybe_unused]] float lv[4][2];   // log2 of the scales of tokens 8 j + 2c + e
+                if constexpr (kScaled) {
+                    float top = 0.f;   // lane's token
+                    for (int gi = 0; gi < (NG == 1 ? 1 : ng); ++gi) top = fmaxf(top, fabsf(ldsf(sv + 4 * (lane * (NG == 1 ? 1 : ng) + gi))));
+                    top = log2_scale(top);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) lv[j][e] = __shfl_sync(0xFFFFFFFFu, top, 8 * j + 2 * c + e);
+                }
                 float alpha[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[n >> 1][j][2 * (n & 1)], s[n >> 1][j][2 * (n & 1) + 1]));
+                    for (int j = 0; j < 4; ++j) {
+                        const float u0 = s[n >> 1][j][2 * (n & 1)], u1 = s[n >> 1][j][2 * (n & 1) + 1];
+                        if constexpr (kScaled) mx = fmaxf(mx, fmaxf(u0 + lv[j][0], u1 + lv[j][1]));
+                        else mx = fmaxf(mx, fmaxf(u0, u1));
+                    }
                     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
                     alpha[n] = 1.f;
@@ -624,7 +646,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, RT>::kThreads, 1)
                         m[n] = mx;
                     }
                     // (a row that has seen nothing keeps m = -inf and weights 2^(-inf) = 0; a NaN logit gives NaN)
-                    const float mb = m[n] == -INFINITY ? 0.f : m[n] - kLogF;
+                    const float mb = m[n] == -INFINITY ? 0.f : m[n] - kUp;
                     float sum = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)

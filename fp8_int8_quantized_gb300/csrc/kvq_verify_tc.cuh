@@ -9,6 +9,8 @@
 // with P = P_hi + P_lo in fp16 pairs (~22 bits) side by side as columns, summed
 // when the accumulator is read: V is read once for both.  (The rows as M, 128
 // of them whatever the chunk, would cost four times the products at 32 rows.)
+// P carries the token's own V scale, and a row's running maximum is that of the
+// weight with it (log2_scale in kvq_verify.cuh).
 //
 // Roles of the CTA's 20 warps (one CTA per SM; registers moved between the
 // warpgroups with setmaxnreg):
@@ -337,7 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kCols = kUsed <= 256 ? 256 : 512;
     static_assert(kUsed <= 512, "tensor memory");
     constexpr uint32_t kIdS = idesc(128, RT, 0, 0), kIdO = idesc(128, 2 * RT, 1, 1), kIdLo = idesc(128, RT, 1, 1);
-    constexpr float kLogF = kScaled && NG == 1 ? (I4 ? -6.f : -2.f) : kUp;   // see kvq_verify.cuh (group scales are in V)
     constexpr float kScaleUp = I4 ? 4.f : 64.f, kMaxScale = 65504.f / kScaleUp;   // V's group scales
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* l_s = reinterpret_cast<float*>(sm + L::kL);
         float* f_s = reinterpret_cast<float*>(sm + L::kF);
         int* row_s = reinterpret_cast<int*>(sm + L::kRow);
-        const float* mm = m_s + g * RT;   // the rows' maxima (less kLogF): weights are 2^(z - mm)
+        const float* mm = m_s + g * RT;   // the rows' maxima (less kUp): weights are 2^(z - mm)
         const float s_fp8 = (!kScaled && a.scale) ? __ldg(a.scale) : 1.0f;
         const float qk = a.sm_scale * s_fp8 * kLog2e;
         const int lbs = 31 - __clz(BS);
@@ -826,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = x0; x < seg; x += 2) {
                 const int j = js + x, t = (w.t + x) * kTok + tok;
                 float k[NG], vs = vn;   // of this thread's token
+                const float lv = kScaled && NG == 1 ? log2_scale(vs) : 0.f;   // (group scales are in V)
 #pragma unroll
                 for (int i = 0; i < NG; ++i) k[i] = qk * kn[i];
                 if (kScaled) {
@@ -898,13 +900,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int r = 0; r < 16; r += 2) top = fmax3(top, s[r], s[r + 1]);
                 }
                 bool held = RT <= 32;
-                if (bar_any(1 + g, 128, top > kLazy + kLogF)) {
-                    // New maxima over the tile's tokens.
+                if (bar_any(1 + g, 128, top + lv > kLazy + kUp)) {
+                    // New maxima over the tile's tokens, of the weights with V's scale.
                     held = false;
 #pragma unroll 1
                     for (int c0 = 0; c0 < RT; c0 += 16) {
                         float v[16];
-                        logits(v, c0, [](int) { return kLogF; });
+                        logits(v, c0, [&](int) { return kUp - lv; });
 #pragma unroll
                         for (int r = 0; r < 16; ++r) v[r] = warp_max(v[r]);
                         if (lane == 0) {

@@ -326,7 +326,7 @@ KVQ_API size_t kvq_verify_workspace_size(int32_t batch, int32_t num_q_heads, int
  *     gets zeros.  A masked token never reaches a query, whatever it holds (NaN
  *     codes and scales included).
  *     A value of V above 65504 in magnitude (bf16 input quantized online may hold
- *     one) gives infinity or NaN to the queries that see it.
+ *     one) may give infinity or NaN to the queries that see it.
  *   max_query_len: an upper bound of every n_b, at most 64; max_context_len: of
  *     every context_lens[b], at most 2^30.  batch at most 4096.
  *   out rows of sequences with n_b > context_lens[b], a length above its bound,

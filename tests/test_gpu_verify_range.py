@@ -72,6 +72,17 @@ def test_one_token_takes_most_of_the_softmax(fmt, group, d, hkv, g, n, kind):
     check(b, b.run(), range(4))
 
 
+@pytest.mark.parametrize("kind", [1.0, 2.0 ** -7, 2.0 ** -10, 2.0 ** -14, 2.0 ** -20, "mixed", "sink"])
+@pytest.mark.parametrize("fmt,group,d", [("int8", 0, 128), ("int4", 0, 128), ("int8", 0, 64), ("int4", 0, 64), ("int8", 16, 64),
+                                         ("int4", 32, 64), ("int8", 32, 128), ("int4", 64, 128), ("e4m3", 0, 128), ("e5m2", 0, 64)])
+@pytest.mark.parametrize("hkv,g,n", [(2, 2, 3), (1, 8, 4), (1, 8, 7)])
+def test_small_and_mixed_values(fmt, group, d, hkv, g, n, kind):
+    ctx = [8000, 700, 90, n]
+    b = Batch(ctx, [n] * 4, hkv, g, d, 16, fmt, group, tree=True, seed=31, outliers=False)
+    fill(b, kind)
+    check(b, b.run(), range(4))
+
+
 @pytest.mark.parametrize("fmt,group,d", [("e4m3", 0, 128), ("int8", 0, 128), ("int4", 32, 128), ("e5m2", 0, 64), ("int8", 16, 64)])
 @pytest.mark.parametrize("g,n", [(2, 4), (8, 4), (8, 7)])
 def test_large_logits_of_a_draft_leave_its_siblings_alone(fmt, group, d, g, n):
@@ -86,3 +97,21 @@ def test_large_logits_of_a_draft_leave_its_siblings_alone(fmt, group, d, g, n):
     out = b.run(tree_mask=mask)
     own = torch.arange(16 * n, device="cuda") % n == 2
     assert torch.equal(out[~own], clean[~own]) and not torch.equal(out[own], clean[own])
+
+
+@pytest.mark.parametrize("fmt,group,d", [("int8", 0, 128), ("int4", 0, 128), ("int8", 0, 64), ("int4", 16, 64)])
+@pytest.mark.parametrize("g,n", [(2, 4), (8, 4), (8, 7)])
+def test_large_values_of_a_draft_leave_its_siblings_alone(fmt, group, d, g, n):
+    """Draft 2's V grows by 2000, from rows of 2^-7: the maxima count V's scale, of the rows that see it only."""
+    b = Batch([3000 + i for i in range(16)], [n] * 16, 8, g, d, 16, fmt, group, tree=True, seed=33, outliers=False)
+    fill(b, 2.0 ** -7)
+    mask = R.signed([1 | 1 << i for i in range(n)] * 16).cuda()
+    clean = b.run(tree_mask=mask)
+    at = torch.tensor([sum(b.ctx[:i + 1]) - n + 2 for i in range(16)], device="cuda")
+    b.v[at] = (b.v[at].float() * 2000).half()
+    kvq.append(b.k, b.v, b.cache, b.slots, b.scale)
+    out = b.run(tree_mask=mask)
+    own = torch.arange(16 * n, device="cuda") % n == 2
+    assert torch.equal(out[~own], clean[~own]) and not torch.equal(out[own], clean[own])
+    b.masks = [[1 | 1 << i for i in range(n)]] * 16
+    check(b, out, [0, 15])
