@@ -860,7 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
-                if ((w.t + x + 1) * kTok > P) {
+                const bool masked = (w.t + x + 1) * kTok > P;
+                if (masked) {
                     // A tile that reaches into the chunk: its logits are masked in
                     // tensor memory (-inf where a row does not see the token), and
                     // the code below is the same for every tile.  A scale of V that
@@ -917,11 +918,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     bar_any(1 + g, 128, false);
                     if (tok < RT) {
-                        // Only rows that exceed their own maximum by 2^kLazy: what the others hold does not
-                        // depend on tokens they do not see.  (One that has seen nothing, or only NaN, keeps kNone.)
+                        // All rows, so that fewer tiles come here (E4M3, 32 x 8192 tokens: 101.7 us, 103.6 when only
+                        // rows that exceed their own by 2^kLazy are raised); but in a tile that reaches into the chunk
+                        // only those: what a row holds must not depend on tokens it does not see.
+                        // (One that has seen nothing, or only NaN, keeps kNone.)
                         const float old = mm[tok];
                         const float tile = fmaxf(fmaxf(mx_s[tok], mx_s[RT + tok]), fmaxf(mx_s[2 * RT + tok], mx_s[3 * RT + tok]));
-                        const float mn = tile > old + kLazy ? tile : old;
+                        const float mn = tile > old + (masked ? kLazy : 0.f) ? tile : old;
                         f_s[g * RT + tok] = fast_exp2(old - mn);
                         m_s[g * RT + tok] = mn;
                     }
