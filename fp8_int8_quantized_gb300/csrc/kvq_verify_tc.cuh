@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             landed();
             uint32_t gs1[NG], gs2[NG];   // V's scales of this token x 2^2 (INT4) or 2^6 (INT8), as two fp16 terms, each twice
+            [[maybe_unused]] bool unusable = false;
             if constexpr (NG > 1) {
                 const uint4 raw = lds128(gring + gr * L::kGroups);
                 if (++gr == L::kVUnits) gr = 0;
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a draft token's scale that is not finite in fp16 must not reach the rows that do not see it
                     if (t >= draft0 && !(fabsf(s) < kMaxScale)) {
                         s = 0.f;
-                        nan_seen[seg & 3] = 1;
+                        unusable = true;
                     }
                     const float up = s * kScaleUp;
                     gs1[i] = pack_f16x2(up, up);
@@ -678,6 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (j >= 2 && !wait(VFREE0 + sl, ((j - 2) >> 1) & 1)) break;
+            // Noted only now: P V of tile j - 2 is done, so the segment before its own has ended (OFREE) and
+            // with it every reset of this slot; before the wait segment seg - 4 may still be at its end.
+            if (NG > 1 && unusable) nan_seen[seg & 3] = 1;
             {
                 const uint32_t src = ring + ru * L::kUnit + lane * RB + (sw << 4);   // chunk c: src ^ 16 c
                 const uint32_t dst = sb + L::kV + sl * L::kVBuf + (tok >> 3) * 1024 + (tok & 7) * 144;   // (row, chunk tok % 8)

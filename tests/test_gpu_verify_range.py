@@ -115,3 +115,45 @@ def test_large_values_of_a_draft_leave_its_siblings_alone(fmt, group, d, g, n):
     assert torch.equal(out[~own], clean[~own]) and not torch.equal(out[own], clean[own])
     b.masks = [[1 | 1 << i for i in range(n)]] * 16
     check(b, out, [0, 15])
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("fmt,group,bad", [(f, w, x) for f in ("int8", "int4") for w in (0, 32, 64) for x in (NAN, INF, 1e6)]
+                         + [("e4m3", 0, NAN), ("e5m2", 0, NAN)])
+@pytest.mark.parametrize("g,n", [(2, 4), (8, 4)])
+def test_bad_drafts_of_many_short_sequences(fmt, group, bad, g, n):
+    """Segments of one tile each, about twenty per CTA: every fifth sequence holds a draft whose V is not finite, or
+    with a scale of 10^6.  With group scales (a scale beyond fp16) its own row is NaN or infinite every time; a finite
+    row scale gives what 64 bits give, infinite from fp16's largest value on.  Nothing else changes."""
+    ctx = [20 + 7 * i % 109 for i in range(400)]
+    b = Batch(ctx, [n] * 400, 8, g, 128, 16, fmt, group, tree=True, seed=34, outliers=False)
+    b.masks = [[1 | 1 << i for i in range(n)]] * 400
+    mask = R.signed(b.masks[0] * 400).cuda()
+    clean = b.run(tree_mask=mask)
+    at = torch.tensor([sum(ctx[:i + 1]) - n + 2 for i in range(0, 400, 5)], device="cuda")
+    blk, row = b.slots[at] // 16, b.slots[at] % 16
+    if fmt[0] == "e":
+        b.cache.v_codes[blk, :, row] = 0x7F
+    else:
+        b.cache.v_scales[blk, :, row] = bad
+    own = torch.zeros(400, n, dtype=torch.bool, device="cuda")
+    own[::5, 2] = True
+    own = own.flatten()
+    for _ in range(5):
+        out = b.run(tree_mask=mask)
+        assert torch.equal(out[~own], clean[~own])
+        if group or bad != 1e6:
+            assert not torch.isfinite(out[own]).any()
+    if not group and bad == 1e6:
+        for i in range(0, 400, 50):
+            k, v = b.kv(i)
+            s = b.slots[sum(ctx[:i]):sum(ctx[:i + 1])]
+            unit = b.cache.v_scales[s // 16, :, s % 16].double()
+            q = b.q[b.start[i]:b.start[i + 1]].double()
+            o, bound = VB.attention(q, k, v, unit, v.abs() / unit[..., None], b.masks[i], 128 ** -0.5, ctx[i] - n, False)
+            got = out[b.start[i]:b.start[i + 1]].double()
+            fits, beyond = o.abs() + bound < 65504, o.abs() - bound > 65520
+            assert ((got - o).abs() <= bound)[fits].all() and torch.isinf(got[beyond]).all() and beyond.any()
+    assert kvq.device_error_check() == (0, 0)
