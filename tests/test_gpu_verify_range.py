@@ -36,7 +36,10 @@ def fill(b, kind):
 
 
 def check(b, out, seqs):
+    in_v = b.group and b.group < b.d and b.d == 128 and len(b.ctx) <= 1024   # tcgen05: V carries its group scales
     for i in seqs:
+        if not b.n[i]:
+            continue
         k, v = b.kv(i)
         at = sum(b.ctx[:i])
         s = b.slots[at:at + b.ctx[i]]
@@ -45,19 +48,18 @@ def check(b, out, seqs):
         else:
             sc = b.cache.v_scales[s // b.bs, :, s % b.bs].double().reshape(*v.shape[:2], -1)
             full = sc.repeat_interleave(b.d // sc.shape[-1], -1)
-            if sc.shape[-1] > 1 and b.d == 128:   # the scale is in V
+            if in_v:
                 unit, codes = torch.ones_like(v[..., 0]), v.abs()
             else:
                 unit, codes = sc.amax(-1), torch.where(full > 0, v.abs() / full, 0.0)
         q = b.q[b.start[i]:b.start[i + 1]].double()
-        pair = b.group and b.group < b.d and b.d == 128
-        o, bound = VB.attention(q, k, v, unit, codes, b.masks[i], b.d ** -0.5, b.ctx[i] - b.n[i], pair)
+        o, bound = VB.attention(q, k, v, unit, codes, b.masks[i], b.d ** -0.5, b.ctx[i] - b.n[i], in_v)
         got = out[b.start[i]:b.start[i + 1]].double()
         assert torch.isfinite(got).all()
         far = ((got - o).abs() / bound).max().item()
         assert far <= 1.0, (i, b.ctx[i], far)
         e = VB.rms(got - o)
-        assert e <= VB.rms_bound(o), (i, b.ctx[i], e / VB.rms(o))
+        assert e <= VB.rms_bound(o, b.ctx[i]), (i, b.ctx[i], e / VB.rms(o))
     assert kvq.device_error_check() == (0, 0)
 
 
@@ -157,3 +159,16 @@ def test_bad_drafts_of_many_short_sequences(fmt, group, bad, g, n):
             fits, beyond = o.abs() + bound < 65504, o.abs() - bound > 65520
             assert ((got - o).abs() <= bound)[fits].all() and torch.isinf(got[beyond]).all() and beyond.any()
     assert kvq.device_error_check() == (0, 0)
+
+
+@pytest.mark.parametrize("fmt,group,d,hkv,g,n,ctx", [
+    ("e4m3", 0, 128, 1, 8, 4, [20011]), ("e5m2", 0, 64, 2, 1, 3, [9000, 31]), ("int8", 0, 128, 2, 4, 8, [4999, 1, 5000]),
+    ("int4", 32, 128, 1, 8, 5, [12345, 800]), ("e4m3", 0, 128, 4, 8, 13, [3000, 2999, 50]), ("int8", 32, 64, 4, 8, 3, [9000] * 30),
+    ("int8", 32, 128, 8, 8, 4, [12000] * 8), ("int8", 64, 128, 4, 8, 2, [9000] * 16), ("int4", 64, 128, 8, 8, 4, [12000] * 8),
+    ("int8", 0, 128, 8, 8, 8, [9000] * 8), ("int4", 0, 128, 8, 8, 4, [12000] * 8), ("int4", 0, 64, 8, 8, 4, [12000] * 8),
+    ("int8", 0, 128, 8, 1, 5, [5, 0, 9000, 130, 0, 0, 4097, 128, 129, 1, 20000, 640, 0]),
+    ("int4", 32, 128, 8, 8, 4, [5, 0, 9000, 130, 0, 0, 4097, 128, 129, 1, 20000, 640, 0])])
+def test_long_contexts_to_the_rounding_of_the_output(fmt, group, d, hkv, g, n, ctx):
+    """Contexts split over the GPU, held to a bound that a lost tile of 32 tokens breaks."""
+    b = Batch(ctx, [min(n, c) for c in ctx], hkv, g, d, 64, fmt, group, tree=False, seed=35, outliers=False)
+    check(b, b.run(), range(min(3, len(ctx))) if len(ctx) < 9 else [1, 2, 6, 10, 11] if len(ctx) < 14 else [0, len(ctx) - 1])

@@ -31,17 +31,18 @@ def attention(q, k, v, s, codes, masks, sm_scale, prefix, pair):
     n, Hq, D = q.shape
     ctx, Hkv = k.shape[:2]
     sees = visible(masks, n, ctx, prefix, q.device)
-    o, bound = torch.zeros(n, Hq, D, dtype=torch.float64, device=q.device), None
+    o = torch.zeros(n, Hq, D, dtype=torch.float64, device=q.device)
     bound = torch.zeros_like(o)
     for h in range(Hq):
-        kk, vv, kv = k[:, h // (Hq // Hkv)], v[:, h // (Hq // Hkv)], h // (Hq // Hkv)
+        kv = h // (Hq // Hkv)
+        kk, vv = k[:, kv], v[:, kv]
         z = ((q[:, h] @ kk.T) * sm_scale).masked_fill(~sees, -torch.inf)
         w = torch.where(sees.any(-1)[:, None], torch.softmax(z, -1), 0.0)
         A = torch.where(sees, (q[:, h].abs() @ kk.abs().T) * abs(sm_scale), 0.0).amax(-1)[:, None]
         o[:, h] = w @ vv
         top = (w * s[:, kv]).amax(-1)[:, None]
         bound[:, h] = (2.0 ** -11 * o[:, h].abs() + (5 if pair else 1) * 2.0 ** -25
-                       + (w @ vv.abs()) * (coefficient(A, ctx)) + 2.0 ** -31 * top * (sees.double() @ codes[:, kv]))
+                       + (w @ vv.abs()) * coefficient(A, ctx) + 2.0 ** -31 * top * (sees.double() @ codes[:, kv]))
     return o, bound
 
 
@@ -54,8 +55,8 @@ def rms(x):
     return x.square().mean().sqrt().item()
 
 
-def rms_bound(o):
-    """Root mean square error over a sequence: the output's rounding is at most 2^-11 of every element; the
-    other errors are per token, of either sign, and sum like the terms of o itself: at most the coefficient
-    above (below 2^-11 for ctx <= 8192 and A <= 28) of its root mean square."""
-    return 2.0 ** -10 * rms(o) + 2.0 ** -25
+def rms_bound(o, ctx, A=28.0):
+    """Root mean square error over a sequence of ctx tokens with sum |q k| sm_scale <= A: the output's rounding is at
+    most 2^-11 of every element; the other errors are per token, of either sign, and sum like the terms of o itself,
+    at most the coefficient above of its root mean square."""
+    return (2.0 ** -11 + coefficient(A, ctx)) * rms(o) + 2.0 ** -25
