@@ -317,8 +317,8 @@ def decode_attention_static_scratch(q: torch.Tensor, cache: KVCache, block_table
 
 # The calls below check their tensors inline and in one condition each: the
 # binding's own time is most of a small call's.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)   # looked up on use: a torch built without CUDA has no such name
 
 
 def _refuse(t, dtype, name: str, device: int, shape=None) -> None:
@@ -362,7 +362,7 @@ def _on(device: int, stream, call):
     allocates then belongs to that stream)."""
     if device < 0:
         raise TypeError("the cache is not on a CUDA device")
-    if stream is None and device == _current_device():
+    if stream is None and device == torch._C._cuda_getDevice():
         return call(_raw_stream(device))
     with torch.cuda.device(device), torch.cuda.stream(stream):   # (stream None: the current one)
         return call(_raw_stream(device))
