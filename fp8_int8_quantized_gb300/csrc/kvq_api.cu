@@ -61,6 +61,23 @@ int sm_count(int dev) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two sets of n rows of 16-bit elements (x_row elements, x_stride >= x_row apart, from x on; y
+// likewise) share any.  Rows of one buffer side by side, such as a fused QKV buffer's, do not.
+bool rows_overlap(const void* x, int64_t x_stride, int64_t x_row, const void* y, int64_t y_stride, int64_t y_row, int64_t n) {
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2;
+    if (d >= (n - 1) * x_stride + x_row || -d >= (n - 1) * y_stride + y_row) return false;
+    const auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    if (x_stride == y_stride) {   // row t of y starts at element r of x's place t + j
+        const int64_t j = floor_div(d, x_stride), r = d - j * x_stride;
+        return (r < x_row && j < n && -j < n) || (r + y_row > x_stride && j + 1 < n && -(j + 1) < n);
+    }
+    for (int64_t t = 0; t < n; ++t) {   // the last row of x that starts before the end of y's row t
+        const int64_t a = d + t * y_stride, u = std::min(n - 1, floor_div(a + y_row - 1, x_stride));
+        if (u >= 0 && u * x_stride + x_row > a) return true;
+    }
+    return false;
+}
+
 kvq_status check_cache(const kvq_cache* c, int32_t fmt) {
     if (!c) return KVQ_ERR_INVALID_ARG;
     if (fmt != KVQ_E4M3 && fmt != KVQ_E5M2 && fmt != KVQ_INT8 && fmt != KVQ_INT4) return KVQ_ERR_INVALID_ARG;
@@ -335,11 +352,12 @@ kvq_status kvq_append_rotary(const void* q, int64_t q_stride, const void* k, int
         if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16)) return KVQ_ERR_INVALID_ARG;
         const int64_t row = num_q_heads * D;
         if (q_stride % 8 || q_out_stride % 8 || q_stride < row || q_out_stride < row) return KVQ_ERR_INVALID_ARG;
-        // in place (the same fp16 rows) or apart
-        const char *x = static_cast<const char*>(q), *y = static_cast<const char*>(q_out);
-        const int64_t xn = 2 * ((num_tokens - 1) * q_stride + row), yn = 2 * ((num_tokens - 1) * q_out_stride + row);
-        const bool same = x == y && (q_stride == q_out_stride || num_tokens == 1) && dtype == KVQ_F16;
-        if (!same && x < y + yn && y < x + xn) return KVQ_ERR_INVALID_ARG;
+        // in place (the same fp16 rows) or apart; K and V are read while q_out is written
+        const bool same = q == q_out && (q_stride == q_out_stride || num_tokens == 1) && dtype == KVQ_F16;
+        if ((!same && rows_overlap(q, q_stride, row, q_out, q_out_stride, row, num_tokens)) ||
+            rows_overlap(k, k_stride, Hkv * D, q_out, q_out_stride, row, num_tokens) ||
+            rows_overlap(v, v_stride, Hkv * D, q_out, q_out_stride, row, num_tokens))
+            return KVQ_ERR_INVALID_ARG;
     }
     int dev;
     if (!current_device(&dev)) return KVQ_ERR_CUDA;

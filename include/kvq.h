@@ -288,8 +288,9 @@ KVQ_API kvq_status kvq_prefill_attention(const void* q, const kvq_cache* cache,
  *     with interleaved != 0.  A pair (x, y) becomes (fl(fl(x c) - fl(y s)),
  *     fl(fl(y c) + fl(x s))) in fp32, every product and sum rounded.
  *   q_out: fp16 rows, tokens q_out_stride elements apart: the rotated Q rounded
- *     once.  q_out may be q itself (fp16, the same stride); else the two must
- *     not overlap, and q_out must not overlap k or v.
+ *     once.  q_out may be q itself (fp16, the same stride); else its rows must
+ *     share nothing with q's, and never with k's or v's (KVQ_ERR_INVALID_ARG;
+ *     rows side by side in one buffer share nothing).
  *   cache, slot_mapping, scale, fmt: as in kvq_append; K is quantized from the
  *     fp32 value of its rotation (not rounded to fp16 first), V as it comes.
  *     Slots of one call must differ (else the slot's row is undefined).

@@ -2,6 +2,8 @@
 import subprocess
 import sys
 
+import pytest
+
 
 def test_the_package_imports_where_torch_has_no_cuda():
     """A torch built without CUDA lacks torch._C's CUDA functions; calls raise there, the import does not."""
@@ -17,3 +19,30 @@ def test_the_package_imports_where_torch_has_no_cuda():
             "    print('refused')\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
+
+
+def rotary_status(out, out_stride, q=(1 << 20, 512), k=(2 << 20, 256), v=(3 << 20, 256), T=8):
+    """kvq_append_rotary with 4 q-heads and 2 kv-heads of 128 channels; nothing is launched where it refuses."""
+    import ctypes
+
+    import fp8_int8_quantized_gb300 as kvq
+    kvq.build()
+    c = kvq.KvqCacheDesc(16, 16, None, None, 8, 16, 2, 128, kvq.E4M3, 0)
+    return kvq.lib().kvq_append_rotary(*q, *k, *v, 0, 4, ctypes.byref(c), 16, T, 16, 1, None, 16, 100, 128, 0, None, kvq.E4M3,
+                                       out, out_stride, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=2 << 20, out_stride=512),                        # over k
+    dict(out=3 << 20, out_stride=512),                        # over v
+    dict(out=(2 << 20) + 2 * (7 * 256 + 248), out_stride=512),   # over the last elements of k's last row
+    dict(out=(3 << 20) - 2 * (7 * 512 + 8), out_stride=512),     # its last row's last elements over v's first
+    dict(out=(2 << 20) - 2 * (511 - 7), out_stride=512, T=1),
+    dict(out=1 << 20, out_stride=520), dict(out=1 << 20, out_stride=504 + 16 + 512),   # over q, other rows
+    # one fused buffer [q | k | v], rows of 1024: over k, over v, into the next token's q
+    dict(q=(1 << 20, 1024), k=((1 << 20) + 1024, 1024), v=((1 << 20) + 1536, 1024), out=(1 << 20) + 1024, out_stride=1024),
+    dict(q=(1 << 20, 1024), k=((1 << 20) + 1024, 1024), v=((1 << 20) + 1536, 1024), out=(1 << 20) + 1040, out_stride=1024),
+    dict(q=(1 << 20, 1024), k=((1 << 20) + 1024, 1024), v=((1 << 20) + 1536, 1024), out=(1 << 20) + 16, out_stride=1024),
+    dict(q=(1 << 20, 1024), k=((1 << 20) + 1024, 1024), v=((1 << 20) + 1536, 1024), out=(1 << 20) - 1024, out_stride=1024)])
+def test_rotated_queries_are_refused_over_the_rows_that_are_read(kw):
+    assert rotary_status(**kw) == 1
