@@ -391,8 +391,10 @@ kvq_status kvq_append_rotary(const void* q, int64_t q_stride, const void* k, int
 
 size_t kvq_verify_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                  int32_t max_query_len, int32_t max_context_len, int32_t fmt) {
-    if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_context_len <= 0) return 0;
-    if (num_q_heads % num_kv_heads || max_query_len <= 0 || max_query_len > kvq::kMaxVerifyQuery) return 0;
+    if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_query_len <= 0 || max_context_len <= 0) return 0;
+    if (num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 8 || max_query_len > kvq::kMaxVerifyQuery) return 0;
+    if (batch > kMaxBatch || max_context_len > 1 << 30 || (head_dim != 64 && head_dim != 128)) return 0;
+    if (fmt != KVQ_E4M3 && fmt != KVQ_E5M2 && fmt != KVQ_INT8 && fmt != KVQ_INT4) return 0;
     int dev = 0;
     if (!current_device(&dev)) dev = 0;
     size_t most = 0;   // with and without group scales

@@ -46,3 +46,12 @@ def rotary_status(out, out_stride, q=(1 << 20, 512), k=(2 << 20, 256), v=(3 << 2
     dict(q=(1 << 20, 1024), k=((1 << 20) + 1024, 1024), v=((1 << 20) + 1536, 1024), out=(1 << 20) - 1024, out_stride=1024)])
 def test_rotated_queries_are_refused_over_the_rows_that_are_read(kw):
     assert rotary_status(**kw) == 1
+
+
+@pytest.mark.parametrize("sizes", [(2, 18, 2, 128, 4, 1000, 1), (4097, 8, 2, 128, 4, 1000, 1), (2, 8, 2, 96, 4, 1000, 1), (2, 8, 2, -128, 4, 1000, 1),
+                                   (2, 8, 2, 128, 4, (1 << 30) + 1, 1), (2, 8, 2, 128, 4, 1000, 9), (2, (1 << 31) - 1, 1, 128, 64, 1000, 1)])
+def test_no_workspace_for_what_is_not_taken(sizes):
+    import fp8_int8_quantized_gb300 as kvq
+    kvq.build()
+    assert kvq.lib().kvq_verify_workspace_size(*sizes) == 0
+    assert kvq.lib().kvq_verify_workspace_size(2, 16, 2, 128, 4, 1 << 30, 1) > 0
