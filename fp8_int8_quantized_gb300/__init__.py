@@ -362,6 +362,8 @@ def _on(device: int, stream, call):
     allocates then belongs to that stream)."""
     if device < 0:
         raise TypeError("the cache is not on a CUDA device")
+    if stream is not None and stream.device.index != device:
+        raise ValueError(f"stream: expected one of cuda:{device}, the cache's device, got {stream.device}")
     if stream is None and device == torch._C._cuda_getDevice():
         return call(_raw_stream(device))
     with torch.cuda.device(device), torch.cuda.stream(stream):   # (stream None: the current one)

@@ -55,3 +55,14 @@ def test_no_workspace_for_what_is_not_taken(sizes):
     kvq.build()
     assert kvq.lib().kvq_verify_workspace_size(*sizes) == 0
     assert kvq.lib().kvq_verify_workspace_size(2, 16, 2, 128, 4, 1 << 30, 1) > 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call would run on the current stream of the cache's device instead."""
+    from types import SimpleNamespace
+
+    import torch
+
+    import fp8_int8_quantized_gb300 as kvq
+    with pytest.raises(ValueError, match="cuda:1"):
+        kvq._on(0, SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7), lambda s: s)
