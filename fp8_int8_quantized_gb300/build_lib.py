@@ -7,6 +7,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -18,6 +19,18 @@ LIB = os.path.join(HERE, "libkvq.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
+
+# Kernels that deal their launch's registers out among their warpgroups (setmaxnreg) run only with exactly
+# these registers per thread; the library refuses to launch another build, this one to make it.
+REGISTERS = {"verify_tc_kernel": 96}
+
+
+def check_registers(text: str) -> None:
+    """Raises RuntimeError where a kernel of REGISTERS was compiled to other registers (ptxas -v's report)."""
+    for name, used in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", text, re.S):
+        for kernel, want in REGISTERS.items():
+            if kernel in name and int(used) != want:
+                raise RuntimeError(f"{name}: {used} registers per thread, its warpgroups are dealt {want}")
 
 
 def nvcc() -> str:
@@ -45,15 +58,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         o = os.path.join(BUILD, os.path.basename(s)[:-3] + ".o")
         objs.append(o)
         if force or _stale(o, [s] + headers):
-            cmd = [nvcc()] + ARCH + FLAGS + os.environ.get("KVQ_NVCC_FLAGS", "").split() + ["-c", s, "-o", o]
-            if verbose:
-                cmd.insert(1, "-Xptxas=-v")
-            jobs.append(cmd)
+            jobs.append([nvcc(), "-Xptxas=-v"] + ARCH + FLAGS + os.environ.get("KVQ_NVCC_FLAGS", "").split() + ["-c", s, "-o", o])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+        try:
+            check_registers(r.stdout + r.stderr)
+        except RuntimeError:
+            os.remove(cmd[-1])   # the next build compiles it again
+            raise
         return r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:

@@ -66,3 +66,26 @@ def test_a_stream_of_another_device_is_refused():
     import fp8_int8_quantized_gb300 as kvq
     with pytest.raises(ValueError, match="cuda:1"):
         kvq._on(0, SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7), lambda s: s)
+
+
+def test_the_build_checks_registers():
+    from fp8_int8_quantized_gb300 import build_lib as b
+    report = ("ptxas info    : Compiling entry function '{}' for 'sm_103a'\n"
+              "ptxas info    : Function properties for {}\n    0 bytes stack frame\n"
+              "ptxas info    : Used {} registers, used 16 barriers, 448 bytes smem\n")
+    tc, other = "_ZN3kvq6verify2tc16verify_tc_kernelILi3ELi64ELi1EEE", "_ZN3kvq6verify13verify_kernelILi3E"
+    b.check_registers(report.format(tc, tc, 96) + report.format(other, other, 255))
+    with pytest.raises(RuntimeError, match="88 registers"):
+        b.check_registers(report.format(other, other, 255) + report.format(tc, tc, 96) + report.format(tc, tc, 88))
+
+
+def test_a_kernel_with_other_registers_is_not_built(tmp_path, monkeypatch):
+    """Through the build itself, on a source of its own whose kernel bears the checked name."""
+    from fp8_int8_quantized_gb300 import build_lib as b
+    (tmp_path / "csrc").mkdir()
+    (tmp_path / "csrc" / "k.cu").write_text("__global__ void verify_tc_kernel(float* x) { x[threadIdx.x] += 1.f; }\n")
+    for name, value in (("CSRC", tmp_path / "csrc"), ("BUILD", tmp_path / "b"), ("LIB", tmp_path / "l.so")):
+        monkeypatch.setattr(b, name, str(value))
+    with pytest.raises(RuntimeError, match="registers per thread"):
+        b.build()
+    assert not (tmp_path / "l.so").exists() and not (tmp_path / "b" / "k.o").exists()
