@@ -191,12 +191,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ float warp_max(float x) {   // over the warp; NaN does not count
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 enum Bar : int {
     KFULL0, KFULL1,   // dequant -> MMA: K in tensor memory (128)
     KFREE0, KFREE1,   // MMA -> dequant (commit of S)
