@@ -488,7 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kTok / 16; ++kk, dv += 2048 >> 4, dp += 2048 >> 4) {
                             mma_ss(o, dv, dp, kIdO, j - js >= 2 || kk > 0);
-                            if (NG > 1) mma_ss(o, dv + (kTileV >> 4), dp, kIdLo, 1u);   // V's residual times P's value
+                            // V's residual times P's value, to the columns of P's residual: a sum of small terms rounds
+                            // less, and the values' columns take half as many additions
+                            if (NG > 1) mma_ss(o + RT, dv + (kTileV >> 4), dp, kIdLo, 1u);
                         }
                         commit(&bars[VFREE0 + sl]);
                     }

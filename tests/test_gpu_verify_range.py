@@ -172,3 +172,23 @@ def test_long_contexts_to_the_rounding_of_the_output(fmt, group, d, hkv, g, n, c
     """Contexts split over the GPU, held to a bound that a lost tile of 32 tokens breaks."""
     b = Batch(ctx, [min(n, c) for c in ctx], hkv, g, d, 64, fmt, group, tree=False, seed=35, outliers=False)
     check(b, b.run(), range(min(3, len(ctx))) if len(ctx) < 9 else [1, 2, 6, 10, 11] if len(ctx) < 14 else [0, len(ctx) - 1])
+
+
+@pytest.mark.parametrize("fmt,group", [("int4", 32), ("int8", 64)])
+def test_long_sums_of_group_scaled_values(fmt, group):
+    """How many results are the 64-bit ones rounded to fp16.  A sum on the tensor cores loses half a step of 2^-23 per
+    addition on average (it truncates), always to the same side: after n additions it is off by n 2^-24, and a result lies
+    that near a border of fp16's steps (2^-10.5 of it on average) with a chance of n 2^-13.5.  n: 8 products of 16 tokens
+    per tile of 128, half of a CTA's tiles; the products with V's residuals have a sum of their own."""
+    n, ctx = 4, 115000
+    b = Batch([ctx] * 3, [n] * 3, 8, 8, 128, 64, fmt, group, tree=False, seed=36, outliers=False)
+    out = b.run().double()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    additions = 8 * -(-3 * 8 * -(-ctx // 128) // sms) / 2
+    k, v = b.kv(1)
+    q, off = b.q[n:2 * n].double(), 0
+    sees = VB.visible(b.masks[1], n, ctx, ctx - n, "cuda")
+    for h in range(64):
+        w = torch.softmax((q[:, h] @ k[:, h // 8].T * 128 ** -0.5).masked_fill(~sees, -torch.inf), -1)
+        off += (out[n:2 * n, h] != (w @ v[:, h // 8]).half().double()).sum().item()
+    assert off / (64 * n * 128) <= additions * 2.0 ** -13.5
