@@ -232,8 +232,13 @@ struct Smem {
     static constexpr uint32_t kBar = kRow + RT * 4;
     static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
-    static constexpr uint32_t kNan = kAbort + 4;                       // int [4]: NaN codes or scales met in segment s % 4
-    static constexpr uint32_t kScan = kNan + 16;                       // int S[B + 1], context lengths [B]
+    // NaN codes or scales met in segment s, in slot s % kSlots, which the end of segment s - kSlots has to have
+    // reset before.  A code of tile j is noted once P V of tile j - 2 is done, so segment s - 3 has ended:
+    // 4 slots.  A scale is noted before that wait, when P V of tile j - 4 is and segment s - 5 has ended: 8
+    // (4 slots and the note kept until after the wait: 354 us in the INT4 case above, with 8 344).
+    static constexpr int kSlots = NG > 1 ? 8 : 4;
+    static constexpr uint32_t kNan = kAbort + 4;                       // int [kSlots]
+    static constexpr uint32_t kScan = kNan + 4 * kSlots;               // int S[B + 1], context lengths [B]
     static constexpr uint32_t bytes(int B) { return kScan + (2 * B + 1) * 4 + 1024; }
     static_assert(kUnits >= 1 && bytes(kMaxBatch) + 512 <= 227 * 1024, "shared memory of one CTA");
 };
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     verify_tc_kernel(const VerifyArgs a, const VerifyPlan plan) {
     using L = Smem<FMT, RT, NG>;
     constexpr bool I4 = FMT == INT4, kScaled = FMT == INT8 || FMT == INT4;
-    constexpr int RB = row_bytes(FMT, D), NU = L::kUnits;
+    constexpr int RB = row_bytes(FMT, D), NU = L::kUnits, kSlots = L::kSlots;
     // tensor memory: K 2 x 64 columns (fp16 pairs), O 2 x 2 RT, and S in two buffers per stream where
     // they fit (S of the stream's next tile then runs under the softmax of this one), NG x RT each
     constexpr int SB = 128 + 4 * NG * RT + 4 * RT <= 512 ? 4 : 2;   // S of tile j: buffer j % SB
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars[i], c128 ? 128u : i == QFULL0 || i == QFULL1 ? 32u : i == OFREE ? 256u : i == OFINAL ? 2u : 1u);
         }
         *abort = 0;
-        for (int i = 0; i < 4; ++i) nan_seen[i] = 0;
+        for (int i = 0; i < kSlots; ++i) nan_seen[i] = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -656,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             landed();
             uint32_t gs1[NG], gs2[NG];   // V's scales of this token x 2^2 (INT4) or 2^6 (INT8), as two fp16 terms, each twice
-            [[maybe_unused]] bool unusable = false;
             if constexpr (NG > 1) {
                 const uint4 raw = lds128(gring + gr * L::kGroups);
                 if (++gr == L::kVUnits) gr = 0;
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a draft token's scale that is not finite in fp16 must not reach the rows that do not see it
                     if (t >= draft0 && !(fabsf(s) < kMaxScale)) {
                         s = 0.f;
-                        unusable = true;
+                        nan_seen[seg & (kSlots - 1)] = 1;
                     }
                     const float up = s * kScaleUp;
                     gs1[i] = pack_f16x2(up, up);
@@ -675,9 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (j >= 2 && !wait(VFREE0 + sl, ((j - 2) >> 1) & 1)) break;
-            // Noted only now: P V of tile j - 2 is done, so the segment before its own has ended (OFREE) and
-            // with it every reset of this slot; before the wait segment seg - 4 may still be at its end.
-            if (NG > 1 && unusable) nan_seen[seg & 3] = 1;
             {
                 const uint32_t src = ring + ru * L::kUnit + lane * RB + (sw << 4);   // chunk c: src ^ 16 c
                 const uint32_t dst = sb + L::kV + sl * L::kVBuf + (tok >> 3) * 1024 + (tok & 7) * 144;   // (row, chunk tok % 8)
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (m.x | m.y | m.z | m.w) {
                             auto clean = [](uint32_t u, uint32_t w) { return u & ~((w >> 7) * 255u); };
                             sts128(src ^ (c << 4), clean(y.x, m.x), clean(y.y, m.y), clean(y.z, m.z), clean(y.w, m.w));
-                            nan_seen[seg & 3] = 1;
+                            nan_seen[seg & (kSlots - 1)] = 1;
                         }
                     }
                 }
@@ -1038,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned long long nan_rows = 0;   // rows whose channel is NaN
             const int ch = quad * 32 + lane;   // this thread's row of O^T
             const int d = I4 ? (ch & ~7) | ((ch & 1) << 2) | ((ch & 7) >> 1) : ch;   // its channel
-            if ((!kScaled || NG > 1) && nan_seen[segno & 3]) {
+            if ((!kScaled || NG > 1) && nan_seen[segno & (kSlots - 1)]) {
                 for (int t = max(P, w.t * kTok); t < min(sq.ctx, (w.t + seg) * kTok); ++t) {
                     const int bid = __ldg(bt + (t >> lbs));
                     if (bid < 0 || bid >= a.cache.num_blocks) continue;
@@ -1107,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_before();
             asm volatile("bar.sync 3, 256;" ::: "memory");   // maxima, sums and factors read by everyone
             if (tid == 0) {
-                nan_seen[segno & 3] = 0;
+                nan_seen[segno & (kSlots - 1)] = 0;
                 if (js + seg == cnt) {   // the last segment: parts of it that later CTAs hold
                     *hdr = make_int4(w.b, w.kvh, cls, w.t == 0 ? sh.parts : 0);
                 }
