@@ -29,8 +29,14 @@ VerifyPlan plan_verify(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
         return p;
     }
     p.warps = 8;
-    // A partial result is `rows` x head_dim fp32 values; with a range per warp
-    // every warp may leave two.
+    // A partial result is `rows` x head_dim fp32 values; with a range per warp every warp may leave
+    // two, with a range per CTA every (sequence, kv-head) it meets ends in a merge of its 8 warps.
+    // Range per warp / per CTA, us, head_dim 64, 8 kv-heads, E4M3, 8 or 2 rows (tiles per warp):
+    //   8 sequences of 2432 (4)    21.2 / 18.0     8 x 4864 (8)   26.7 / 22.8     8 x 7296 (12)  32.1 / 29.0
+    //   128 x 333 .. 1000 (27)     40.5 / 62.6     64 x 1333 .. 4000 (53) 63.7 / 74.9
+    //   1024 x 83 .. 250 (54)      89.8 / 197      4096 x 20 .. 60 (54)   181 / 704
+    // so 12 tiles per warp part the two where a batch is large; with fewer pairs than CTAs a range per CTA
+    // stays 5 to 10% ahead beyond them (8 x 29184, 48 tiles per warp: 81.5 / 77.6).
     p.team = tiles >= (int64_t)sms * p.warps * 12 ? 1 : p.warps;
     const int64_t want = p.team == 1 ? sms : (tiles + p.warps - 1) / p.warps;
     p.ctas = (int32_t)std::max<int64_t>(std::min<int64_t>(sms, want), std::min(p.row_tiles, sms));

@@ -45,9 +45,10 @@
 // is ~1400 (8-bit codes).  Measured, the reduction included, calls back to back
 // over three sets of inputs (the first after a flush of L2):
 //   E4M3, 32 x 8192 tokens, 64 / 8 heads, 4 queries (32 rows)       101 us, 5.4 TB/s (115)
-//   E5M2, 24 x 515 .. 8191, 32 / 8 heads, trees of 9 .. 16 (64)      83 us, 2.6 TB/s (88)
+//   E5M2, 24 x 515 .. 8191, 32 / 8 heads, trees of 9 .. 16 (64)      82 us, 2.7 TB/s (88)
 //   INT8, 16 x 4096, 40 / 40 heads, 8 queries (16)                  122 us, 5.7 TB/s (137)
-//   INT4, 32-channel groups, 3 x ~115000, 64 / 8, 5 .. 7 (2 x 32)   356 us, 1.25 TB/s (355)
+//   INT4, 32-channel groups, 3 x ~115000, 64 / 8, 5 .. 7 (2 x 32)   343 us, 1.29 TB/s
+//   INT4, a scale per row, 32 x 8192, 64 / 8, 4 (32)                123 us, 2.4 TB/s
 //   E5M2, one sequence of 1000, 32 / 8, 4 queries (16)               (17 us)
 #pragma once
 

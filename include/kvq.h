@@ -314,8 +314,17 @@ KVQ_API size_t kvq_verify_workspace_size(int32_t batch, int32_t num_q_heads, int
 
 /* Attention of a short chunk of new tokens per sequence -- 1 to 64, such as
  * drafts under verification -- over the paged cache, the contexts split over
- * the whole GPU (kvq_prefill_attention walks a context with one CTA per 256
- * rows: right for long chunks, slow for short ones on long contexts).
+ * the whole GPU.  kvq_prefill_attention gives the same for causal chunks: it
+ * walks a context with one CTA per 256 rows (queries x q-heads of a kv-head),
+ * this call reads it once per 64 rows (32 with group scales at head_dim 128, or
+ * at head_dim 64).  Up to 64 rows this call was the faster one or even, above
+ * that it depends on how many (sequence, kv-head) pairs there are for prefill's
+ * CTAs.  E4M3, head_dim 128, 8 kv-heads of 8 q-heads, this call / prefill, us:
+ *    rows                  64           128          256          512
+ *    1 x 65536 tokens      54 / 1167    82 / 1177    141 / 1323   262 / 1374
+ *    8 x 8192              52 / 166     84 / 167     151 / 182    290 / 184
+ *    32 x 8192             150 / 332    279 / 335    545 / 364    1087 / 714
+ *    32 x 1024             47 / 45      77 / 47      135 / 61     270 / 121
  *   q, query_start, context_lens, block_tables, scale, fmt, sm_scale, out: as
  *     in kvq_prefill_attention; the chunk's own K/V are in the cache, at the
  *     last n_b of the context_lens[b] tokens.  q-group at most 8.
